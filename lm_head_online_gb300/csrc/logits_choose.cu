@@ -71,10 +71,11 @@ __device__ __forceinline__ int64_t token_of(uint64_t key) {
 constexpr uint32_t kMonoNegInf = 0x007FFFFFu;                                       // mono_of(-inf)
 constexpr uint64_t kLowestKey = static_cast<uint64_t>(kMonoNegInf + 1) << 32;       // above every -inf
 
-// Fold of a thread's U vectors, whose maximum is vm, into (m, s).  exp(z - m) is
-// taken as 2^(z log2 e - m log2 e) in one multiply-add; where m itself is so
-// large that m log2 e overflows (a row filled with the type's lowest value, a
-// common mask) the difference is taken first.
+// Fold of a thread's U vectors, whose maximum is vm, into (m, s).  The difference z - m is
+// taken first and then scaled: its two roundings are relative to it, so a term's error
+// does not grow with the logits, and the maximum's own term is 1.  (2^(z log2 e - m log2 e)
+// in one multiply-add would leave the rounding of m log2 e in every exponent, half an ulp
+// of 1.44 m: 8e-7 at 31, nats from 1e8 on, and a sum out of range from 1e10 on.)
 template <typename E, int U>
 __device__ __forceinline__ void fold(MS& a, const uint4 (&r)[U], float vm) {
   constexpr int N = Elt<E>::kPerVec;
@@ -82,36 +83,25 @@ __device__ __forceinline__ void fold(MS& a, const uint4 (&r)[U], float vm) {
     a.s *= ex2_approx((a.m - vm) * kLog2e);
     a.m = vm;
   }
-  if (fabsf(a.m) < 1e38f) {
-    const float o = -a.m * kLog2e;
-    const uint64_t k2 = f32x2(kLog2e, kLog2e), o2 = f32x2(o, o);
-    uint64_t acc0 = f32x2(a.s, 0.f), acc1 = f32x2(0.f, 0.f);
+  const float ref = a.m == -INFINITY ? 0.f : a.m;  // nothing but -inf or NaN so far
+  const uint64_t ref2 = f32x2(ref, ref), k2 = f32x2(kLog2e, kLog2e);
+  uint64_t acc0 = f32x2(a.s, 0.f), acc1 = f32x2(0.f, 0.f);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[N];
-      Elt<E>::unpack(r[u], v);
+  for (int u = 0; u < U; ++u) {
+    float v[N];
+    Elt<E>::unpack(r[u], v);
 #pragma unroll
-      for (int i = 0; i < N; i += 4) {
-        float p, q;
-        f32x2_split(fma_f32x2(f32x2(v[i], v[i + 1]), k2, o2), p, q);
-        acc0 = add_f32x2(acc0, f32x2(ex2_approx(p), ex2_approx(q)));
-        f32x2_split(fma_f32x2(f32x2(v[i + 2], v[i + 3]), k2, o2), p, q);
-        acc1 = add_f32x2(acc1, f32x2(ex2_approx(p), ex2_approx(q)));
-      }
-    }
-    float lo, hi;
-    f32x2_split(add_f32x2(acc0, acc1), lo, hi);
-    a.s = lo + hi;
-  } else {  // nothing but -inf or NaN so far, or an extreme maximum
-    const float ref = a.m == -INFINITY ? 0.f : a.m;
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      float v[N];
-      Elt<E>::unpack(r[u], v);
-#pragma unroll
-      for (int i = 0; i < N; ++i) a.s += ex2_approx((v[i] - ref) * kLog2e);
+    for (int i = 0; i < N; i += 4) {
+      float p, q;
+      f32x2_split(mul_f32x2(sub_f32x2(f32x2(v[i], v[i + 1]), ref2), k2), p, q);
+      acc0 = add_f32x2(acc0, f32x2(ex2_approx(p), ex2_approx(q)));
+      f32x2_split(mul_f32x2(sub_f32x2(f32x2(v[i + 2], v[i + 3]), ref2), k2), p, q);
+      acc1 = add_f32x2(acc1, f32x2(ex2_approx(p), ex2_approx(q)));
     }
   }
+  float lo, hi;
+  f32x2_split(add_f32x2(acc0, acc1), lo, hi);
+  a.s = lo + hi;
 }
 
 // A row seen as 16-byte vectors on the 16-byte grid: vector q holds the elements
