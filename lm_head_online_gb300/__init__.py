@@ -252,8 +252,38 @@ def _on(*tensors):
     return _STAY if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
 
 
-def workspace(nbytes: int, device=None) -> torch.Tensor:
-    """Zero-filled device workspace (torch allocations are 512-byte aligned)."""
+def _under(stream, device):
+    """Context in which a call given ``stream`` allocates and fills what it was not
+    given: with that stream the current one, so that the fill comes before the call's
+    kernels and the memory is not handed out again before they are over."""
+    if not isinstance(stream, torch.cuda.Stream):
+        handle = _stream(stream)  # 0 and 1: the legacy default stream
+        stream = torch.cuda.default_stream(device) if handle in (0, 1) else torch.cuda.ExternalStream(handle, device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _under(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _flat(x, target, stream):
+    """Tokens of [batch, seq] inputs one after the other (copies, where the layout asks
+    for them)."""
+    if stream is not None:
+        with _under(stream, x.device):
+            return _flat(x, target, None)
+    return (x.reshape(-1, x.shape[-1]) if x.dim() == 3 else x), (target.reshape(-1) if target.dim() == 2 else target)
+
+
+def workspace(nbytes: int, device=None, stream=None) -> torch.Tensor:
+    """Zero-filled device workspace (torch allocations are 512-byte aligned), zeroed on
+    ``stream`` (the current one when None)."""
+    if stream is not None:
+        with _under(stream, device):
+            return workspace(nbytes, device)
     return torch.zeros(max(int(nbytes), 256), dtype=torch.uint8, device=device or "cuda")
 
 
@@ -286,9 +316,9 @@ def ce_fwd_f32(logits, target, loss=None, ws=None, stream=None):
         raise ValueError("target must have T entries")
     dev = _cuda_device(loss, ws, logits, target)
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=dev)
+        loss = _empty(1, torch.float32, dev, stream)
     if ws is None:
-        ws = workspace(lib.ce_workspace_bytes(T, V), dev)
+        ws = workspace(lib.ce_workspace_bytes(T, V), dev, stream)
     with _on(logits, target, loss, ws):
         _check(lib.ce_fwd_f32(pl, pt, T, V, _dev(loss, "loss", torch.float32), _dev(ws, "ws", torch.uint8),
                               ws.numel(), _stream(stream)), "ce_fwd_f32")
@@ -324,7 +354,7 @@ def ce_fwd_sbv_bf16(logits, target, loss=None, stream=None):
     if tuple(target.shape) != (S, B):
         raise ValueError("target must be [S, B]")
     if loss is None:
-        loss = torch.empty((S, B), dtype=torch.float32, device=_cuda_device(logits, target))
+        loss = _empty((S, B), torch.float32, _cuda_device(logits, target), stream)
     with _on(logits, target, loss):
         _check(lib.ce_fwd_sbv_bf16(pl, pt, S, B, V, _dev(loss, "loss", torch.float32), _stream(stream)),
                "ce_fwd_sbv_bf16")
@@ -346,7 +376,7 @@ def ce_partials_sbv_bf16(logits_local, target, vocab_start, partials=None, strea
     if tuple(target.shape) != (S, B):
         raise ValueError("target must be [S, B]")
     if partials is None:
-        partials = torch.empty((3, S, B), dtype=torch.float32, device=_cuda_device(logits_local, target))
+        partials = _empty((3, S, B), torch.float32, _cuda_device(logits_local, target), stream)
     if tuple(partials.shape) != (3, S, B):
         raise ValueError("partials must be [3, S, B]")
     with _on(logits_local, target, partials):
@@ -368,7 +398,7 @@ def ce_partials_f32(logits_local, target, vocab_start, partials=None, stream=Non
     if target.shape[0] != T:
         raise ValueError("target must be [T]")
     if partials is None:
-        partials = torch.empty((3, T), dtype=torch.float32, device=_cuda_device(logits_local, target))
+        partials = _empty((3, T), torch.float32, _cuda_device(logits_local, target), stream)
     if tuple(partials.shape) != (3, T):
         raise ValueError("partials must be [3, T]")
     with _on(logits_local, target, partials):
@@ -389,7 +419,7 @@ def ce_merge_partials(partials, target, V, loss=None, stream=None):
     if tuple(target.shape) != (S, B):
         raise ValueError("target must be [S, B]")
     if loss is None:
-        loss = torch.empty((S, B), dtype=torch.float32, device=partials.device)
+        loss = _empty((S, B), torch.float32, partials.device, stream)
     with _on(partials, target, loss):
         _check(lib.ce_merge_partials(pp, k, pt, S, B, int(V), _dev(loss, "loss", torch.float32, 2), _stream(stream)),
                "ce_merge_partials")
@@ -406,13 +436,13 @@ def ce_fwd_bwd_f32(logits, target, grad_scale=1.0, loss=None, dlogits=None, ws=N
     if target.shape[0] != T:
         raise ValueError("target must have T entries")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=logits.device)
+        loss = _empty(1, torch.float32, logits.device, stream)
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _empty(logits.shape, logits.dtype, logits.device, stream)
     if tuple(dlogits.shape) != (T, V):
         raise ValueError("dlogits must be [T, V]")
     if ws is None:
-        ws = workspace(lib.ce_workspace_bytes(T, V), logits.device)
+        ws = workspace(lib.ce_workspace_bytes(T, V), logits.device, stream)
     with _on(logits, target, loss, dlogits, ws):
         _check(lib.ce_fwd_bwd_f32(pl, pt, T, V, float(grad_scale), _dev(loss, "loss", torch.float32),
                                   _dev(dlogits, "dlogits", torch.float32), _dev(ws, "ws", torch.uint8), ws.numel(),
@@ -436,9 +466,9 @@ def ce_fwd_bwd_sbv_bf16(logits, target, dloss=None, grad_scale=1.0, loss=None, d
         if tuple(dloss.shape) != (S, B):
             raise ValueError("dloss must be [S, B]")
     if loss is None:
-        loss = torch.empty((S, B), dtype=torch.float32, device=logits.device)
+        loss = _empty((S, B), torch.float32, logits.device, stream)
     if dlogits is None:
-        dlogits = torch.empty_like(logits)
+        dlogits = _empty(logits.shape, logits.dtype, logits.device, stream)
     with _on(logits, target, loss, dlogits, dloss):
         _check(lib.ce_fwd_bwd_sbv_bf16(pl, pt, S, B, V, pd, float(grad_scale), _dev(loss, "loss", torch.float32),
                                        _dev(dlogits, "dlogits", torch.bfloat16, 3), _stream(stream)),
@@ -453,10 +483,7 @@ def flce_fwd_bf16(x, W, target, loss=None, ws=None, stream=None):
     [batch, seq] int64.  ``ws[:4*T]`` (float32) holds the per-token losses.
     """
     lib = load()
-    if x.dim() == 3:
-        x = x.reshape(-1, x.shape[-1])
-    if target.dim() == 2:
-        target = target.reshape(-1)
+    x, target = _flat(x, target, stream)
     px = _dev(x, "x", torch.bfloat16, 2)
     pw = _dev(W, "W", torch.bfloat16, 2)
     pt = _dev(target, "target", torch.int64, 1)
@@ -465,9 +492,9 @@ def flce_fwd_bf16(x, W, target, loss=None, ws=None, stream=None):
     if W.shape[1] != H or target.shape[0] != T:
         raise ValueError("shape mismatch: x [T,H], W [V,H], target [T]")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=x.device)
+        loss = _empty(1, torch.float32, x.device, stream)
     if ws is None:
-        ws = workspace(lib.flce_workspace_bytes(T, H, V), x.device)
+        ws = workspace(lib.flce_workspace_bytes(T, H, V), x.device, stream)
     with _on(x, W, target, loss, ws):
         _check(lib.flce_fwd_bf16(px, pw, pt, T, H, V, _dev(loss, "loss", torch.float32), _dev(ws, "ws", torch.uint8),
                                  ws.numel(), _stream(stream)), "flce_fwd_bf16")
@@ -482,10 +509,7 @@ def flce_fwd_bwd_bf16(x, W, target, grad_scale=1.0, loss=None, dx=None, dW=None,
     """Mean cross-entropy of z = x W^T and the gradients of grad_scale * loss:
     returns (loss fp32 [1], dx fp32 [T, H], dW fp32 [V, H])."""
     lib = load()
-    if x.dim() == 3:
-        x = x.reshape(-1, x.shape[-1])
-    if target.dim() == 2:
-        target = target.reshape(-1)
+    x, target = _flat(x, target, stream)
     px = _dev(x, "x", torch.bfloat16, 2)
     pw = _dev(W, "W", torch.bfloat16, 2)
     pt = _dev(target, "target", torch.int64, 1)
@@ -494,13 +518,13 @@ def flce_fwd_bwd_bf16(x, W, target, grad_scale=1.0, loss=None, dx=None, dW=None,
     if W.shape[1] != H or target.shape[0] != T:
         raise ValueError("shape mismatch: x [T,H], W [V,H], target [T]")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=x.device)
+        loss = _empty(1, torch.float32, x.device, stream)
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        dx = _empty((T, H), torch.float32, x.device, stream)
     if dW is None:
-        dW = torch.empty((V, H), dtype=torch.float32, device=x.device)
+        dW = _empty((V, H), torch.float32, x.device, stream)
     if ws is None:
-        ws = workspace(lib.flce_bwd_workspace_bytes(T, H, V), x.device)
+        ws = workspace(lib.flce_bwd_workspace_bytes(T, H, V), x.device, stream)
     with _on(x, W, target, loss, dx, dW, ws):
         _check(lib.flce_fwd_bwd_bf16(px, pw, pt, T, H, V, float(grad_scale), _dev(loss, "loss", torch.float32),
                                      _dev(dx, "dx", torch.float32, 2), _dev(dW, "dW", torch.float32, 2),
@@ -535,13 +559,13 @@ def flce_cpo_fwd_bf16(x, W, target, beta=0.1, alpha=1.0, loss=None, logps=None, 
     pw = _dev(W, "W", torch.bfloat16, 2)
     pt = _dev(target, "target", torch.int64, 2)
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=x.device)
+        loss = _empty(1, torch.float32, x.device, stream)
     if logps is None:
-        logps = torch.empty(B, dtype=torch.float32, device=x.device)
+        logps = _empty(B, torch.float32, x.device, stream)
     if logps.numel() != B or loss.numel() < 1:
         raise ValueError("logps must hold B floats, loss at least one")
     if ws is None:
-        ws = workspace(lib.flce_cpo_workspace_bytes(B, S, H, V), x.device)
+        ws = workspace(lib.flce_cpo_workspace_bytes(B, S, H, V), x.device, stream)
     with _on(x, W, target, loss, logps, ws):
         _check(lib.flce_cpo_fwd_bf16(px, pw, pt, B, S, H, V, float(beta), float(alpha), _dev(loss, "loss", torch.float32),
                                      _dev(logps, "logps", torch.float32, 1), _dev(ws, "ws", torch.uint8), ws.numel(),
@@ -559,17 +583,17 @@ def flce_cpo_fwd_bwd_bf16(x, W, target, beta=0.1, alpha=1.0, grad_scale=1.0, los
     pw = _dev(W, "W", torch.bfloat16, 2)
     pt = _dev(target, "target", torch.int64, 2)
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=x.device)
+        loss = _empty(1, torch.float32, x.device, stream)
     if logps is None:
-        logps = torch.empty(B, dtype=torch.float32, device=x.device)
+        logps = _empty(B, torch.float32, x.device, stream)
     if dx is None:
-        dx = torch.empty((B, S, H), dtype=torch.float32, device=x.device)
+        dx = _empty((B, S, H), torch.float32, x.device, stream)
     if dW is None:
-        dW = torch.empty((V, H), dtype=torch.float32, device=x.device)
+        dW = _empty((V, H), torch.float32, x.device, stream)
     if logps.numel() != B or loss.numel() < 1 or tuple(dx.shape) != (B, S, H) or tuple(dW.shape) != (V, H):
         raise ValueError("output shapes: loss [1], logps [B], dx [B, S, H], dW [V, H]")
     if ws is None:
-        ws = workspace(lib.flce_cpo_bwd_workspace_bytes(B, S, H, V), x.device)
+        ws = workspace(lib.flce_cpo_bwd_workspace_bytes(B, S, H, V), x.device, stream)
     with _on(x, W, target, loss, logps, dx, dW, ws):
         _check(lib.flce_cpo_fwd_bwd_bf16(px, pw, pt, B, S, H, V, float(beta), float(alpha), float(grad_scale),
                                          _dev(loss, "loss", torch.float32), _dev(logps, "logps", torch.float32, 1),
@@ -592,9 +616,9 @@ def fljsd_fwd_bf16(xs, Ws, xt, Wt, beta=0.5, loss=None, ws=None, stream=None):
     if tuple(xt.shape) != (T, H) or tuple(Ws.shape) != (V, H) or tuple(Wt.shape) != (V, H):
         raise ValueError("shape mismatch: xs, xt [T,H]; Ws, Wt [V,H]")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=xs.device)
+        loss = _empty(1, torch.float32, xs.device, stream)
     if ws is None:
-        ws = workspace(lib.fljsd_workspace_bytes(T, H, V), xs.device)
+        ws = workspace(lib.fljsd_workspace_bytes(T, H, V), xs.device, stream)
     with _on(xs, Ws, xt, Wt, loss, ws):
         _check(lib.fljsd_fwd_bf16(p1, p2, p3, p4, T, H, V, float(beta), _dev(loss, "loss", torch.float32),
                                   _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "fljsd_fwd_bf16")
@@ -622,9 +646,9 @@ def fljsd_fwd_bf16_ex(xs, Ws, xt, Wt, beta=0.5, temperature=1.0, keep=None, loss
         if keep.shape[0] != T:
             raise ValueError("keep must have T entries")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=xs.device)
+        loss = _empty(1, torch.float32, xs.device, stream)
     if ws is None:
-        ws = workspace(lib.fljsd_workspace_bytes(T, H, V), xs.device)
+        ws = workspace(lib.fljsd_workspace_bytes(T, H, V), xs.device, stream)
     with _on(xs, Ws, xt, Wt, keep, loss, ws):
         _check(lib.fljsd_fwd_bf16_ex(p1, p2, p3, p4, T, H, V, float(beta), float(temperature), pk,
                                      _dev(loss, "loss", torch.float32), _dev(ws, "ws", torch.uint8), ws.numel(),
@@ -657,13 +681,13 @@ def fljsd_fwd_bwd_bf16(xs, Ws, xt, Wt, beta=0.5, temperature=1.0, keep=None, gra
         if keep.shape[0] != T:
             raise ValueError("keep must have T entries")
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=xs.device)
+        loss = _empty(1, torch.float32, xs.device, stream)
     if dxs is None:
-        dxs = torch.empty((T, H), dtype=torch.float32, device=xs.device)
+        dxs = _empty((T, H), torch.float32, xs.device, stream)
     if dWs is None:
-        dWs = torch.empty((V, H), dtype=torch.float32, device=xs.device)
+        dWs = _empty((V, H), torch.float32, xs.device, stream)
     if ws is None:
-        ws = workspace(lib.fljsd_bwd_workspace_bytes(T, H, V), xs.device)
+        ws = workspace(lib.fljsd_bwd_workspace_bytes(T, H, V), xs.device, stream)
     with _on(xs, Ws, xt, Wt, keep, loss, dxs, dWs, ws):
         _check(lib.fljsd_fwd_bwd_bf16(p1, p2, p3, p4, T, H, V, float(beta), float(temperature), pk, float(grad_scale),
                                       _dev(loss, "loss", torch.float32), _dev(dxs, "dxs", torch.float32, 2),
@@ -713,11 +737,11 @@ def flce_partials_bf16(x, W_local, target, vocab_start, partials=None, ws=None, 
     if W_local.shape[1] != H or target.shape[0] != T:
         raise ValueError("shape mismatch: x [T,H], W_local [V_local,H], target [T]")
     if partials is None:
-        partials = torch.empty((3, T), dtype=torch.float32, device=x.device)
+        partials = _empty((3, T), torch.float32, x.device, stream)
     if tuple(partials.shape) != (3, T):
         raise ValueError("partials must be [3, T]")
     if ws is None:
-        ws = workspace(lib.flce_workspace_bytes(T, H, Vl), x.device)
+        ws = workspace(lib.flce_workspace_bytes(T, H, Vl), x.device, stream)
     with _on(x, W_local, target, partials, ws):
         _check(lib.flce_partials_bf16(px, pw, pt, T, H, Vl, int(vocab_start), _dev(partials, "partials", torch.float32, 2),
                                       _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "flce_partials_bf16")
@@ -744,13 +768,13 @@ def flce_shard_bwd_bf16(x, W_local, target, partials, vocab_start, V, grad_scale
     if W_local.shape[1] != H or target.shape[0] != T or tuple(partials.shape[1:]) != (3, T):
         raise ValueError("shape mismatch: x [T,H], W_local [V_local,H], target [T], partials [shards,3,T]")
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.float32, device=x.device)
+        dx = _empty((T, H), torch.float32, x.device, stream)
     if dW is None:
-        dW = torch.empty((Vl, H), dtype=torch.float32, device=x.device)
+        dW = _empty((Vl, H), torch.float32, x.device, stream)
     if tuple(dx.shape) != (T, H) or tuple(dW.shape) != (Vl, H):
         raise ValueError("dx must be [T, H] and dW [V_local, H]")
     if ws is None:
-        ws = workspace(lib.flce_bwd_workspace_bytes(T, H, Vl), x.device)
+        ws = workspace(lib.flce_bwd_workspace_bytes(T, H, Vl), x.device, stream)
     with _on(x, W_local, target, partials, dx, dW, ws, row_w):
         pdx, pdw, pws = _dev(dx, "dx", torch.float32, 2), _dev(dW, "dW", torch.float32, 2), _dev(ws, "ws", torch.uint8)
         if row_w is None:
@@ -782,16 +806,16 @@ def cpo_combine_rows(rows, B, beta=0.1, alpha=1.0, loss=None, logps=None, row_w=
         raise ValueError("rows must hold B sequences of equal length")
     S = n // B
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=rows.device)
+        loss = _empty(1, torch.float32, rows.device, stream)
     if logps is None:
-        logps = torch.empty(B, dtype=torch.float32, device=rows.device)
+        logps = _empty(B, torch.float32, rows.device, stream)
     pw = None
     if row_w is not None:
         pw = _dev(row_w, "row_w", torch.float32, 1)
         if row_w.shape[0] != n:
             raise ValueError("row_w must be [B * S]")
     if ws is None:
-        ws = workspace(lib.cpo_combine_workspace_bytes(B), rows.device)
+        ws = workspace(lib.cpo_combine_workspace_bytes(B), rows.device, stream)
     with _on(rows, loss, logps, ws, row_w):
         _check(lib.cpo_combine_rows(pr, B, S, float(beta), float(alpha), _dev(loss, "loss", torch.float32),
                                     _dev(logps, "logps", torch.float32, 1), pw, _dev(ws, "ws", torch.uint8),
@@ -806,11 +830,11 @@ def fljsd_lse_partials_bf16(xs, Ws_local, xt, Wt_local, temperature=1.0, out=Non
     lib = load()
     ptrs, T, H, Vl = _shard_pair(xs, Ws_local, xt, Wt_local)
     if out is None:
-        out = torch.empty((2, T), dtype=torch.float32, device=xs.device)
+        out = _empty((2, T), torch.float32, xs.device, stream)
     if tuple(out.shape) != (2, T):
         raise ValueError("out must be [2, T]")
     if ws is None:
-        ws = workspace(lib.fljsd_workspace_bytes(T, H, Vl), xs.device)
+        ws = workspace(lib.fljsd_workspace_bytes(T, H, Vl), xs.device, stream)
     with _on(xs, Ws_local, xt, Wt_local, out, ws):
         _check(lib.fljsd_lse_partials_bf16(*ptrs, T, H, Vl, float(temperature), _dev(out, "out", torch.float32, 2),
                                            _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream)),
@@ -826,7 +850,7 @@ def lse_merge_partials(parts, out=None, stream=None):
     if two != 2:
         raise ValueError("parts must be [shards, 2, T]")
     if out is None:
-        out = torch.empty((2, T), dtype=torch.float32, device=parts.device)
+        out = _empty((2, T), torch.float32, parts.device, stream)
     if tuple(out.shape) != (2, T):
         raise ValueError("out must be [2, T]")
     with _on(parts, out):
@@ -847,7 +871,7 @@ def fljsd_terms_bf16(xs, Ws_local, xt, Wt_local, lse, beta=0.5, temperature=1.0,
     if tuple(lse.shape) != (2, T):
         raise ValueError("lse must be [2, T]")
     if out is None:
-        out = torch.empty(T, dtype=torch.float32, device=xs.device)
+        out = _empty(T, torch.float32, xs.device, stream)
     if tuple(out.shape) != (T,):
         raise ValueError("out must be [T]")
     pkl = None
@@ -856,7 +880,7 @@ def fljsd_terms_bf16(xs, Ws_local, xt, Wt_local, lse, beta=0.5, temperature=1.0,
         if kl_local.shape[0] != T:
             raise ValueError("kl_local must be [T]")
     if ws is None:
-        ws = workspace(lib.fljsd_workspace_bytes(T, H, Vl), xs.device)
+        ws = workspace(lib.fljsd_workspace_bytes(T, H, Vl), xs.device, stream)
     with _on(xs, Ws_local, xt, Wt_local, lse, out, ws, kl_local):
         _check(lib.fljsd_terms_bf16(*ptrs, pl, T, H, Vl, float(beta), float(temperature),
                                     _dev(out, "out", torch.float32, 1), pkl, _dev(ws, "ws", torch.uint8), ws.numel(),
@@ -879,13 +903,13 @@ def fljsd_shard_bwd_bf16(xs, Ws_local, xt, Wt_local, lse, kl, beta=0.5, temperat
         raise ValueError("lse must be [2, T] and kl [T]")
     pm = _keep_ptr(keep, T)
     if dx is None:
-        dx = torch.empty((T, H), dtype=torch.float32, device=xs.device)
+        dx = _empty((T, H), torch.float32, xs.device, stream)
     if dW is None:
-        dW = torch.empty((Vl, H), dtype=torch.float32, device=xs.device)
+        dW = _empty((Vl, H), torch.float32, xs.device, stream)
     if tuple(dx.shape) != (T, H) or tuple(dW.shape) != (Vl, H):
         raise ValueError("dx must be [T, H] and dW [V_local, H]")
     if ws is None:
-        ws = workspace(lib.fljsd_bwd_workspace_bytes(T, H, Vl), xs.device)
+        ws = workspace(lib.fljsd_bwd_workspace_bytes(T, H, Vl), xs.device, stream)
     with _on(xs, Ws_local, xt, Wt_local, lse, kl, dx, dW, ws, keep):
         _check(lib.fljsd_shard_bwd_bf16(*ptrs, pl, pk, pm, T, H, Vl, float(beta), float(temperature),
                                         float(grad_scale), _dev(dx, "dx", torch.float32, 2),
@@ -903,9 +927,9 @@ def jsd_merge_terms(terms, keep=None, rows=None, loss=None, stream=None):
     k, T = terms.shape
     pk = _keep_ptr(keep, T)
     if rows is None:
-        rows = torch.empty(T, dtype=torch.float32, device=terms.device)
+        rows = _empty(T, torch.float32, terms.device, stream)
     if loss is None:
-        loss = torch.empty(1, dtype=torch.float32, device=terms.device)
+        loss = _empty(1, torch.float32, terms.device, stream)
     if tuple(rows.shape) != (T,):
         raise ValueError("rows must be [T]")
     with _on(terms, rows, loss, keep):
@@ -921,7 +945,7 @@ def rows_mean(rows, keep=None, out=None, stream=None):
     n = rows.shape[0]
     pk = _keep_ptr(keep, n)
     if out is None:
-        out = torch.empty(1, dtype=torch.float32, device=rows.device)
+        out = _empty(1, torch.float32, rows.device, stream)
     with _on(rows, out, keep):
         _check(lib.rows_mean_f32(pr, n, pk, _dev(out, "out", torch.float32), _stream(stream)), "rows_mean_f32")
     return out
@@ -957,14 +981,14 @@ def head_lora_bf16(x, W, A, B, adapter, scale=None, out=None, dtype=torch.float3
         if scale.shape[0] != n:
             raise ValueError("scale must be [n]")
     if out is None:
-        out = torch.empty((T, V), dtype=dtype, device=x.device)
+        out = _empty((T, V), dtype, x.device, stream)
     if out.dtype not in (torch.float32, torch.bfloat16):
         raise TypeError(f"logits must be float32 or bfloat16, got {out.dtype}")
     po = _dev(out, "out", out.dtype, 2)
     if tuple(out.shape) != (T, V):
         raise ValueError("out must be [T, V]")
     if ws is None:
-        ws = workspace(lib.head_lora_workspace_bytes(T, H, V, r), x.device)
+        ws = workspace(lib.head_lora_workspace_bytes(T, H, V, r), x.device, stream)
     with _on(x, W, A, B, adapter, scale, out, ws):
         _check(lib.head_lora_bf16(px, pw, pa, pb, pi, ps, T, H, V, n, r, po, int(out.dtype == torch.bfloat16),
                                   _dev(ws, "ws", torch.uint8), ws.numel(), _stream(stream)), "head_lora_bf16")
@@ -1014,7 +1038,7 @@ def _logits_process(fn, dtype, logits, prompt, prompt_offsets, output, output_of
         if tuple(mask.shape) != (T, (V + 31) // 32):
             raise ValueError("mask must be [T, ceil(V / 32)]")
     if out is None:
-        out = torch.empty((T, V), dtype=torch.float32, device=logits.device)
+        out = _empty((T, V), torch.float32, logits.device, stream)
     if tuple(out.shape) != (T, V):
         raise ValueError("out must be [T, V]")
     with _on(logits, prompt, prompt_offsets, output, output_offsets, repetition, frequency, presence, bias_tokens, bias,
@@ -1074,14 +1098,14 @@ def _logits_choose(fn, dtype, logits, n, top_k, top_p, noise, token, logprob, be
         if tuple(noise.shape) != (T, n):
             raise ValueError("noise must be [T, n]")
     dev = logits.device
-    token = torch.empty(T, dtype=torch.int64, device=dev) if token is None else token
-    logprob = torch.empty(T, dtype=torch.float32, device=dev) if logprob is None else logprob
-    best = torch.empty((T, n), dtype=torch.int64, device=dev) if best is None else best
-    best_logprob = torch.empty((T, n), dtype=torch.float32, device=dev) if best_logprob is None else best_logprob
+    token = _empty(T, torch.int64, dev, stream) if token is None else token
+    logprob = _empty(T, torch.float32, dev, stream) if logprob is None else logprob
+    best = _empty((T, n), torch.int64, dev, stream) if best is None else best
+    best_logprob = _empty((T, n), torch.float32, dev, stream) if best_logprob is None else best_logprob
     if tuple(best.shape) != (T, n) or tuple(best_logprob.shape) != (T, n):
         raise ValueError("best and best_logprob must be [T, n]")
     if ws is None:
-        ws = workspace(lib.logits_choose_workspace_bytes(T, V, n), dev)
+        ws = workspace(lib.logits_choose_workspace_bytes(T, V, n), dev, stream)
     with _on(logits, top_k, top_p, noise, token, logprob, best, best_logprob, ws):
         _check(getattr(lib, fn)(pl, T, V, n, pk, pp, pn, _per_row(token, "token", torch.int64, T),
                                 _per_row(logprob, "logprob", torch.float32, T), _dev(best, "best", torch.int64, 2),
@@ -1127,7 +1151,7 @@ def probe_read(data: torch.Tensor, segment_bytes: int, out=None, stream=None) ->
         raise ValueError("data must be a whole number of segments")
     n = nbytes // segment_bytes
     if out is None:
-        out = torch.empty(n, dtype=torch.int32, device=data.device)
+        out = _empty(n, torch.int32, data.device, stream)
     _check(load().lmho_probe_read(data.data_ptr(), n, int(segment_bytes), _dev(out, "out", torch.int32, 1),
                                   _stream(stream)), "lmho_probe_read")
     return out
