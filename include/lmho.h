@@ -525,7 +525,8 @@ int fljsd_fwd_bwd_bf16(const uint16_t* xs, const uint16_t* Ws, const uint16_t* x
  *            first use.  Status: lmho_ws_status().
  * Accumulation in fp32; x_t A_a^T enters the second product with 24 significant
  * bits (bf16 logits: 16).  A row depends on its own adapter only: non-finite values in one
- * adapter stay in the rows that ask for it.  Two launches; with more than 128
+ * adapter stay in the rows that ask for it, where an infinite entry of B makes an
+ * infinite logit as x_t A_a^T times it does.  Two launches; with more than 128
  * tokens and 2 to 2048 adapters four, the last three programmatic dependents.
  * ------------------------------------------------------------------------ */
 size_t head_lora_workspace_bytes(int64_t T, int64_t H, int64_t V, int64_t r);

@@ -14,10 +14,13 @@
 // tokens need no sorting; several tiles of mixed tokens are sorted all the same
 // (lora_sort, lora_gather), as each tile then asks for fewer adapters.
 //
-// h is kept as three bf16 numbers, h = h0 + h1 + h2 with h0 = bf16(h), h1 =
-// bf16(h - h0), h2 the rest: 24 significant bits, all of the fp32 sum.  Each
-// multiplies the same B tile in shared memory.  bf16 logits take the first two (16
-// bits, 2^-9 of their own rounding).  The tensor cores cut bits at every
+// h is kept as three bf16 numbers, h = h0 + h1 + h2 with h0 = h cut to bf16, h1 =
+// h - h0 cut to bf16, h2 the rest: 24 significant bits, all of the fp32 sum.  Each
+// multiplies the same B tile in shared memory.  bf16 logits take the first two, the
+// second rounded (16 bits, 2^-7 of their own rounding).  Cut, not rounded: a finite h
+// then has finite parts, and parts of one sign, none of them 0 (in the place of a 0
+// stands h 2^-40), make +-inf of an infinite B as h itself does, where 0 inf or inf -
+// inf would be NaN.  The tensor cores cut bits at every
 // accumulation step (4e-6 of the result over H = 4096 against 5e-7 for fp32 sums),
 // so the accumulator is taken out every few k-blocks (Params::chunk) and summed in
 // fp32 registers, while the next ones run into the other accumulator.
@@ -218,7 +221,8 @@ __global__ void __launch_bounds__(kDownThreads) lora_down(const uint16_t* __rest
                                                           const float* __restrict__ scale, int64_t T, int64_t H,
                                                           int64_t n, int r, int r_blocks, int64_t groups,
                                                           uint16_t* __restrict__ h, LoraTile* __restrict__ plan,
-                                                          const int32_t* __restrict__ order, int tile_rows) {
+                                                          const int32_t* __restrict__ order, int tile_rows,
+                                                          bool two_parts) {
   // The head's kernel starts when every block has said so: with an order, when that
   // and x in it are complete.
   if (order) griddep_wait();
@@ -320,12 +324,15 @@ __global__ void __launch_bounds__(kDownThreads) lora_down(const uint16_t* __rest
     v *= s;
     if (q + j >= r_blocks * kRankBlock) continue;
     uint16_t* to = h + (t0 + tok) * row + (q + j) / kRankBlock * 4 * kRankBlock + j % kRankBlock;
+    const float whole = v;
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
-      const uint32_t b = pack_bf16x2(v, 0.f) & 0xFFFFu;
+      if (v == 0.f) v = whole * 0x1p-40f;
+      const bool last = two_parts && k == 1;
+      const uint32_t b = last ? pack_bf16x2(v, 0.f) & 0xFFFFu : __float_as_uint(v) >> 16;
       const float f = __uint_as_float(b << 16);
       to[k * kRankBlock] = static_cast<uint16_t>(b);
-      v = fabsf(f) < INFINITY ? v - f : 0.f;  // a non-finite h0 carries the whole value
+      v = fabsf(f) < INFINITY ? v - f : 0.f;  // every part of a non-finite h is it
     }
   }
 }
@@ -940,7 +947,7 @@ cudaError_t launch_lora_head(const LoraMaps& m, const LoraArgs& a, const FusedLa
       return e;
   }
   if (cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down, a.x, a.A, a.adapter, a.scale, a.T, a.H, a.n, a.r, c.r_blocks,
-                                         groups, a.h, a.plan, p.order, c.x_rows))
+                                         groups, a.h, a.plan, p.order, c.x_rows, a.out_bf16))
     return e;
   const int grid = static_cast<int>(p.units < static_cast<uint32_t>(L.num_sms) ? p.units : L.num_sms);
   const auto head = a.out_bf16 ? (c.vec_out ? launch_head<uint16_t, true> : launch_head<uint16_t, false>)
