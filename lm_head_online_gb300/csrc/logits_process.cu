@@ -313,7 +313,8 @@ struct Shared {
   int32_t bias_token[kBiasList];  // token - v0, -1 outside the window
   float bias_value[kBiasList];
   uint32_t warp_sum[kT / 32];
-  int repeats;                    // a token has more than one bias
+  int repeats;                    // a token of the window has more than one bias
+  int any_repeats;                // one of an earlier window
 };
 
 // One row's lists, as every helper below takes them.
@@ -342,7 +343,9 @@ struct Row {
 // The biases of the columns: mine(v, at) says whether token v0 + v is this block's
 // now, and at which number it is in hand (kUnlisted: it is in no list).  A token's
 // first entry computes its column: in hand it replaces the value there, else it is
-// stored.  The first of a thread's entries has its logit loaded already.
+// stored.  The first of a thread's entries has its logit loaded already.  Where a token
+// has several biases every entry looks through the list: up to kBiasList entries here,
+// longer lists in repeated_biases.
 constexpr uint32_t kUnlisted = 0xFFFFFFFFu;
 struct FirstBias {
   int64_t token;
@@ -352,6 +355,7 @@ struct FirstBias {
 template <typename E, class F, class C>
 __device__ __forceinline__ void bias_columns(Shared& sh, Row<E>& r, const FirstBias& first, int64_t v0, uint32_t width,
                                              float* value, C&& count_of, F&& mine) {
+  if (sh.repeats && !r.bias_kept) return;
   const int64_t b0 = r.bias.lo + threadIdx.x;
   for (int64_t k = b0; k < r.bias.hi; k += kT) {
     const auto token_at = [&](int64_t i) -> uint64_t {
@@ -413,6 +417,134 @@ __device__ __forceinline__ void list_values(const Row<E>& r, int64_t v0, uint32_
   }
 }
 
+// The biased columns of a row whose list is long and has tokens more than once, after
+// everything else of the row: the work grows with the lists' lengths (times the rounds
+// of `room` / 3 tokens), where a search for every entry's repetitions takes the square
+// (60000 biases, one of them repeated: 4.0 ms and 711).  The biased tokens of this
+// block's words get numbers as the listed ones do, and by these their output counts,
+// whether they are in a list, and the sums of their biases in list order: a warp takes
+// the tokens of every kWarps-th word and walks the list 32 entries at a time.
+constexpr int kWarps = kT / 32;
+constexpr int kWalk = 4;  // entries of a lane in flight
+constexpr uint32_t kSeen = 1u << 31, kSummed = 1u << 30;  // above a count (at most kProcessMaxTokens)
+static_assert(kProcessMaxTokens < kSummed, "a count's bits");
+template <typename E>
+__device__ __noinline__ void repeated_biases(const E* logits, const ProcessArgs& a, int64_t t, int rank, int cluster,
+                                             uint32_t* maps, int words, int room, uint32_t* warp_sum) {
+  const E* in = logits + t * a.V;
+  float* out = a.out + t * a.V;
+  const uint32_t* mask = a.mask ? a.mask + t * a.mask_words : nullptr;
+  const Span prompt = span_of(a.prompt_offsets, t, a.n_prompt), output = span_of(a.output_offsets, t, a.n_output),
+             bias = span_of(a.bias_offsets, t, a.n_bias);
+  const RowRule rule = rule_of(a, t);
+  const uint32_t most = room / 3;
+  uint32_t* marked = maps;
+  uint32_t* number = maps + words;
+  uint32_t* hand = maps + 2 * words;
+  uint32_t* count = hand + most;
+  float* sum = reinterpret_cast<float*>(count + most);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int64_t v0 = 0; v0 < a.V; v0 += static_cast<int64_t>(words) * 32) {
+    const int64_t left = a.V - v0;
+    const uint32_t width = static_cast<uint32_t>(left < words * 32 ? left : words * 32);
+    __syncthreads();
+    for (int i = threadIdx.x; i < words; i += kT) marked[i] = 0;
+    __syncthreads();
+    for (int64_t k = bias.lo + threadIdx.x; k < bias.hi; k += kT) {
+      const uint64_t v = static_cast<uint64_t>(a.bias_tokens[k]) - static_cast<uint64_t>(v0);
+      if (v < width && ((v >> 7) & (cluster - 1)) == static_cast<uint32_t>(rank)) atomicOr(&marked[v >> 5], 1u << (v & 31));
+    }
+    __syncthreads();
+    // numbers in the tokens' order: a round is a range of tokens
+    const int each = (words + kT - 1) / kT, w0 = threadIdx.x * each, w1 = min(w0 + each, words);
+    uint32_t mine = 0;
+    for (int i = w0; i < w1; ++i) mine += __popc(marked[i]);
+    uint32_t upto = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, upto, off);
+      if (lane >= off) upto += o;
+    }
+    if (lane == 31) warp_sum[warp] = upto;
+    __syncthreads();
+    uint32_t total = 0, base = upto - mine;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < warp) base += warp_sum[w];
+      total += warp_sum[w];
+    }
+    for (int i = w0; i < w1; ++i) {
+      number[i] = base;
+      base += __popc(marked[i]);
+    }
+    __syncthreads();
+    for (uint32_t n0 = 0; n0 < total; n0 += most) {
+      const uint32_t n = total - n0 < most ? total - n0 : most;
+      for (int i = threadIdx.x; i < words; i += kT) {
+        uint32_t at = number[i] - n0;
+        for (uint32_t bits = marked[i]; bits; bits &= bits - 1, ++at)
+          if (at < n) {
+            hand[at] = static_cast<uint32_t>(i * 32 + __ffs(bits) - 1);
+            count[at] = 0;
+          }
+      }
+      __syncthreads();
+      const int64_t first = v0 + hand[0];
+      const uint32_t range = hand[n - 1] - hand[0];
+      const auto in_round = [&](int64_t token) {
+        return static_cast<uint64_t>(token) - static_cast<uint64_t>(first) <= range;
+      };
+      const auto place_of = [&](int64_t token) -> uint32_t {  // of a token in that range
+        const uint32_t v = static_cast<uint32_t>(token - v0), bits = marked[v >> 5], bit = 1u << (v & 31);
+        return bits & bit ? number[v >> 5] + __popc(bits & (bit - 1)) - n0 : kUnlisted;
+      };
+      for (int64_t k = prompt.lo + threadIdx.x; k < prompt.hi; k += kT) {
+        const int64_t token = a.prompt[k];
+        const uint32_t at = in_round(token) ? place_of(token) : kUnlisted;
+        if (at < n) atomicOr(&count[at], kSeen);
+      }
+      for (int64_t k = output.lo + threadIdx.x; k < output.hi; k += kT) {
+        const int64_t token = a.output[k];
+        const uint32_t at = in_round(token) ? place_of(token) : kUnlisted;
+        if (at < n) atomicAdd(&count[at], 1u);
+      }
+      for (int64_t k0 = bias.lo; k0 < bias.hi; k0 += 32 * kWalk) {
+        int64_t token[kWalk];
+#pragma unroll
+        for (int j = 0; j < kWalk; ++j) {
+          const int64_t k = k0 + 32 * j + lane;
+          token[j] = k < bias.hi ? a.bias_tokens[k] : -1;
+        }
+#pragma unroll
+        for (int j = 0; j < kWalk; ++j) {
+          const bool may = in_round(token[j]) && ((token[j] >> 5) & (kWarps - 1)) == warp;
+          if (!__any_sync(0xFFFFFFFFu, may)) continue;
+          const uint32_t at = may ? place_of(token[j]) : kUnlisted;
+          const bool ours = at < n;
+          uint32_t same = __match_any_sync(0xFFFFFFFFu, ours ? at : kUnlisted);
+          if (ours && lane == __ffs(same) - 1) {
+            const float* value = a.bias + k0 + 32 * j;
+            const bool more = atomicOr(&count[at], kSummed) & kSummed;
+            float s = more ? __fadd_rn(sum[at], value[lane]) : value[lane];
+            for (same &= same - 1; same; same &= same - 1) s = __fadd_rn(s, value[__ffs(same) - 1]);
+            sum[at] = s;
+          }
+          __syncwarp();
+        }
+      }
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < n; i += kT) {
+        const int64_t v = v0 + hand[i];
+        if (mask && !((__ldg(mask + (v >> 5)) >> (v & 31)) & 1u)) continue;
+        float z = Elt<E>::load1(in + v);
+        const uint32_t c = count[i] & ~(kSeen | kSummed);
+        if (c || (count[i] & kSeen)) z = penalised(z, c, rule);
+        out[v] = scaled(__fadd_rn(z, sum[i]), rule.inverse, rule.temperature);
+      }
+      __syncthreads();
+    }
+  }
+}
+
 // Dynamic shared memory, 32-bit words: a bitmap of the listed tokens and the numbers
 // of its words' first tokens ([words] each, a multiple of 4; the second is a bitmap of
 // the biased tokens first), then [numbered] tokens in hand with their counts and
@@ -428,8 +560,8 @@ constexpr int64_t kPackedCounts = (1 << (32 - kTokenBits)) - 1;
 static_assert(kProcessMaxWords * 32 == 1 << kTokenBits, "a window's token fits");
 
 template <typename E, bool kCluster>
-__global__ void __launch_bounds__(kT, 3) process_lists(const E* __restrict__ logits, const ProcessArgs a, int cluster,
-                                                         int numbered) {
+__global__ void __launch_bounds__(kT, 3) process_lists(const E* __restrict__ logits,
+                                                       const __grid_constant__ ProcessArgs a, int cluster, int numbered) {
   __shared__ Shared sh;
   extern __shared__ __align__(16) uint32_t maps[];
   const int64_t t = blockIdx.x / cluster;
@@ -453,6 +585,7 @@ __global__ void __launch_bounds__(kT, 3) process_lists(const E* __restrict__ log
   const auto word_at = [&](int j) { return 4 * (rank + (j >> 2) * cluster) + (j & 3); };
   const auto owned = [&](uint32_t v) { return !kCluster || ((v >> 7) & (cluster - 1)) == static_cast<uint32_t>(rank); };
 
+  if (threadIdx.x == 0) sh.repeats = sh.any_repeats = 0;
   // windows of the vocabulary: one up to 262144 tokens
   for (int64_t v0 = 0; v0 < a.V; v0 += static_cast<int64_t>(words) * 32) {
     const int64_t left = a.V - v0;
@@ -474,7 +607,10 @@ __global__ void __launch_bounds__(kT, 3) process_lists(const E* __restrict__ log
     FirstBias bias{b0 < r.bias.hi ? a.bias_tokens[b0] : -1, b0 < r.bias.hi ? a.bias[b0] : 0.f, 0.f, true};
     __syncthreads();
     for (int i = threadIdx.x; i < words / 2; i += kT) reinterpret_cast<uint4*>(maps)[i] = make_uint4(0, 0, 0, 0);
-    if (threadIdx.x == 0) sh.repeats = 0;
+    if (threadIdx.x == 0) {
+      sh.any_repeats |= sh.repeats;
+      sh.repeats = 0;
+    }
     __syncthreads();
     marked.each([&](int j, int64_t token) {
       const uint64_t v = static_cast<uint64_t>(token) - static_cast<uint64_t>(v0);
@@ -595,6 +731,8 @@ __global__ void __launch_bounds__(kT, 3) process_lists(const E* __restrict__ log
     }
   }
   r.wait();  // the call is over only when the stream is
+  if (!r.bias_kept && (sh.repeats | sh.any_repeats))
+    repeated_biases(logits, a, t, rank, cluster, maps, words, 2 * numbered, sh.warp_sum);
 }
 
 // ---------------------------------------------------------------- launches
