@@ -526,7 +526,8 @@ int fljsd_fwd_bwd_bf16(const uint16_t* xs, const uint16_t* Ws, const uint16_t* x
  * Accumulation in fp32; x_t A_a^T enters the second product with 24 significant
  * bits (bf16 logits: 16).  A row depends on its own adapter only: non-finite values in one
  * adapter stay in the rows that ask for it, where an infinite entry of B makes an
- * infinite logit as x_t A_a^T times it does.  Two launches; with more than 128
+ * infinite logit as x_t A_a^T times it does.  Equal calls give equal bits; in another
+ * order or beside other tokens a row may round differently.  Two launches; with more than 128
  * tokens and 2 to 2048 adapters four, the last three programmatic dependents.
  * ------------------------------------------------------------------------ */
 size_t head_lora_workspace_bytes(int64_t T, int64_t H, int64_t V, int64_t r);
@@ -585,16 +586,19 @@ int logits_process_bf16(const uint16_t* logits, int64_t T, int64_t V, const int6
  *   best_logprob  [T, n] fp32 device output: z - logsumexp(row); -inf past the last
  *   token         [T] int64 device output: the drawn token.  Of the best, the
  *                 first top_k[t] stay (top_k int64 [T] device; <= 0 or NULL: all
- *                 n), then the shortest prefix whose softmax mass reaches
- *                 top_p[t] (top_p fp32 [T] device; >= 1 or NULL: all; one token
+ *                 n), then the shortest prefix that holds top_p[t] of their
+ *                 softmax mass -- of the tokens that stayed, not of the whole
+ *                 row -- (top_p fp32 [T] device; >= 1 or NULL: all; one token
  *                 always stays); the token is the one of largest
  *                 z + noise[t, rank] (noise fp32 [T, n] device, equal sums by
  *                 rank): with standard Gumbel noise a draw from the softmax of
  *                 those that stayed.  noise NULL: the best token.
  *   logprob       [T] fp32 device output: the drawn token's log-probability in
  *                 the whole row
- *   ws            ws_bytes >= logits_choose_workspace_bytes(T, V, n): a control
- *                 block, the candidates stay in shared memory
+ *   ws            ws_bytes >= logits_choose_workspace_bytes(T, V, n).  Checked
+ *                 like every call's, but neither read nor written: the candidates
+ *                 stay in shared memory and no wait in the kernel can run out, so
+ *                 lmho_ws_status() has nothing to tell of this call
  * A row that holds NaN or +inf: token and best -1, log-probabilities NaN.  A row
  * of -inf only: token and best -1, log-probabilities -inf.  One launch.
  * ------------------------------------------------------------------------ */

@@ -1123,7 +1123,8 @@ def logits_choose_f32(logits, n, top_k=None, top_p=None, noise=None, token=None,
 
     The token is the best one, or with ``noise`` (fp32 [T, n], standard Gumbel) a
     draw among the first ``top_k`` (int64 [T], <= 0: all n) of the best, cut to
-    the shortest prefix whose probability reaches ``top_p`` (fp32 [T])."""
+    the shortest prefix that holds ``top_p`` (fp32 [T]) of their probability --
+    of those tokens', not of the whole row's.  ``ws`` is checked, not used."""
     return _logits_choose("logits_choose_f32", torch.float32, logits, n, top_k, top_p, noise, token, logprob, best,
                           best_logprob, ws, stream)
 

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests import ref_answer as ref
+from tests.test_gpu_head_lora import check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -91,3 +92,17 @@ def test_infinite_h(gpu_lib, bad):
         with np.errstate(invalid="ignore"):
             want = (x[:, 5] * bad)[:, None] * B[0, :, 3][None, :]
         assert np.array_equal(got.double().cpu().numpy(), want, equal_nan=True)
+
+
+@pytest.mark.parametrize("T", [100, 300])
+def test_several_units_repeat_and_stay_within_the_bound_in_any_order(gpu_lib, T):
+    """Blocks with several units of a token tile: equal calls give equal bits; the tokens
+    in another order may round differently, within the same bound."""
+    vals, dev, adapter, scale = make(T, 512, 30011, 9, 16, seed=T)
+    s, ids = torch.from_numpy(scale).cuda(), torch.from_numpy(adapter).cuda()
+    got = gpu_lib.head_lora_bf16(*dev, ids, scale=s)
+    check(got, vals, adapter, scale)
+    assert torch.equal(gpu_lib.head_lora_bf16(*dev, ids, scale=s), got)
+    order = torch.randperm(T, generator=torch.Generator().manual_seed(3)).cuda()
+    mixed = gpu_lib.head_lora_bf16(dev[0][order].contiguous(), *dev[1:], ids[order].contiguous(), scale=s)
+    check(mixed[torch.argsort(order)], vals, adapter, scale)
