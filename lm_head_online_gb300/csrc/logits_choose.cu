@@ -30,8 +30,9 @@
 // and draws.
 // Bound by HBM while the logits stream (256 fp32 rows of 128256: 22 us, 6.0 TB/s), then
 // by the latency of a row's chain (keys, gather, sort, draw: 9 us).  In a queue of
-// calls those rows take 37.5 us with n = 64 (3.5 TB/s), 2048 bf16 rows of 32768 with n
-// = 8 39 us (3.4 TB/s), 300 bf16 rows of 50001 with n = 20 25 us.  With a barrier of the block in every step the first two were 43 and 41 us.
+// calls those rows take 37.2 us with n = 64 (3.5 TB/s), 2048 bf16 rows of 32768 with n
+// = 8 38.9 us (3.4 TB/s), 300 bf16 rows of 50001 with n = 20 22 to 25 us.  With a barrier
+// of the block in every step the first two were 43 and 41 us.
 #include <cmath>
 #include <cstdint>
 
@@ -567,7 +568,9 @@ struct Cut {
   int64_t piece;  // vectors
 };
 // Pieces of a row (a power of two, each of at least one step, a multiple of the
-// block's width): about kWant blocks in all.
+// block's width): about kWant blocks in all, two for every SM.  Rows of 128256 with n = 64
+// take 38.3 us at 300 rows in two pieces each, 38.5 at 303, and 38.4 at 304 in one; 36.8
+// at 256, 43.8 at 400, 56.0 at 607.
 constexpr int64_t kWant = 304;
 Cut cut_rows(int64_t T, int64_t V, int per_vec) {
   const int64_t vecs = (V + per_vec - 1) / per_vec + 1;

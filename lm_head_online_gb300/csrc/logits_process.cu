@@ -23,15 +23,16 @@
 // That chain of dependent steps is bound by latency, its reads (offsets, lists,
 // logits) queueing behind the stream's; what counts is that it ends no later than the
 // stream.  256 bf16 rows of 128256 with 3000 listed tokens each take 49 us (4.0 TB/s;
-// the stream alone 37), 64 fp32 rows with a mask and 950 tokens 22.5 us (18.4; a copy
-// of as many bytes 16.5), 37 fp32 rows of 50001 with 40000 tokens 37 us (10.2), a
-// single row of 128256 with 400 10 us (6.1), calls by themselves.  With the lists read again for every step, 256
-// threads and 4096 tokens in hand those were 67, 25.6, 42 and 13 us; with the
-// tokens found again from the bitmap's bits 54, 25.6, 40 and 13.5.  In one kernel
-// with a word per column in shared memory the first two took 78 and 33 us; with the
-// lists prepared between the chunks of the stream 143 and 53 (every vector's lookup
-// lengthens the chain from its load to its store); with a hash table in the bitmap's
-// place 85 and 31.6 (atomics that return a value cost far more than setting bits).
+// the stream alone 37), 64 fp32 rows with a mask and 950 tokens 22.5 us (18.4), 37 fp32
+// rows of 50001 with 40000 tokens 37 us (10.2), a single row of 128256 with 400 10 us
+// (6.1), calls by themselves; in a queue of calls 49.2 and 18.5 us for the first two,
+// where copies of as many bytes take 32.8 and 13.5.  With the lists read again for every
+// step, 256 threads and 4096 tokens in hand those were 67, 25.6, 42 and 13 us; with the
+// tokens found again from the bitmap's bits 54, 25.6, 40 and 13.5.  In one kernel with a
+// word per column in shared memory the first two took 78 and 33 us; with the lists
+// prepared between the chunks of the stream 143 and 53 (every vector's lookup lengthens
+// the chain from its load to its store); with a hash table in the bitmap's place 85 and
+// 31.6 (atomics that return a value cost far more than setting bits).
 #include <cmath>
 #include <cstdint>
 
@@ -452,7 +453,8 @@ __device__ __noinline__ void repeated_biases(const E* logits, const ProcessArgs&
     __syncthreads();
     for (int64_t k = bias.lo + threadIdx.x; k < bias.hi; k += kT) {
       const uint64_t v = static_cast<uint64_t>(a.bias_tokens[k]) - static_cast<uint64_t>(v0);
-      if (v < width && ((v >> 7) & (cluster - 1)) == static_cast<uint32_t>(rank)) atomicOr(&marked[v >> 5], 1u << (v & 31));
+      if (v < width && ((v >> 7) & (cluster - 1)) == static_cast<uint32_t>(rank))
+        atomicOr(&marked[v >> 5], 1u << (v & 31));
     }
     __syncthreads();
     // numbers in the tokens' order: a round is a range of tokens

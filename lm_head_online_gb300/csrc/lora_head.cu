@@ -33,12 +33,12 @@
 //
 // Few tokens: bound by HBM, W and the adapters' B read once.  The vocab tile is
 // the multiple of 16 that fills whole waves of SMs best.  1 token, H 4096, V 32768:
-// 48 us (5.6 TB/s); 48 tokens of 24 adapters of 16 ranks, V 128256: 199 us (5.9
+// 47.5 us (5.7 TB/s); 48 tokens of 24 adapters of 16 ranks, V 128256: 197 us (6.0
 // TB/s).  Many adapters beside a short W (200 tokens of 64 adapters of 32 ranks, H
-// 2056, V 50001, bf16 logits: 123 us, 3.6 TB/s): bound by the adapters' MMAs and the
+// 2056, V 50001, bf16 logits: 122 us, 3.6 TB/s): bound by the adapters' MMAs and the
 // time to the first of them, 87 us without adapters.  Many tokens (2048 of 4 adapters
 // of 64 ranks, H 4096, V 128256): bound by the tensor cores, 1.41 ms for a call by
-// itself (1.55 PFLOP/s) and 1.58 ms among others, at the power limit's clocks; a
+// itself (1.55 PFLOP/s) and 1.60 ms among others, at the power limit's clocks; a
 // library's product x W^T with bf16 logits and no adapters takes 1.11 and 1.31 ms.
 #include <cmath>
 #include <cstdint>
